@@ -231,12 +231,10 @@ def _run_own(s):
             out_dtype=s["q"].dtype, with_lse=True)
         return out, lse, s["k_pool"], s["v_pool"]
     if s["kind"] == "plan":
-        n_free = s["out"]["n_free"]
         p = fd.fdllm_plan_blocks(s["seq_lens"], s["new"], s["table"], s["page"], s["free"],
-                                 s["n_free"], out={**s["out"], "headroom": n_free,
-                                                   "n_free": torch.empty_like(n_free)})
+                                 s["n_free"], out=s["out"])
         return (p["cu_rows"], p["positions"], p["slots"], p["row_seq"], p["slot_map"],
-                p["seq_lens"], p["granted"], p["headroom"], s["table"])
+                p["seq_lens"], p["granted"], p["n_free"], s["table"])
     p = fd.fdllm_release_blocks(s["seq_lens"], s["new"], s["table"], s["page"], s["free"],
                                 s["n_free"], out=s["out"])
     return p["seq_lens"], p["n_free"], s["free"]
@@ -264,7 +262,8 @@ def _plain_blocks(s):
     need = (after + ps - 1) // ps - held
     upto = torch.cumsum(need, 0)
     granted = (need == 0) | (upto <= n_free)
-    taken = torch.where(granted, upto, 0).amax(0, keepdim=True)
+    # (a request that needs no page is granted after refused ones, whose pages `upto` counts)
+    taken = torch.where(granted & (need > 0), upto, 0).amax(0, keepdim=True)
     page = torch.arange(table.shape[1], device=table.device)
     fresh = (page >= held[:, None]) & (page < (held + need)[:, None]) & granted[:, None]
     at = n_free - 1 - ((upto - need)[:, None] + page - held[:, None])
