@@ -356,6 +356,8 @@ FDLLM_API fdllm_status fdllm_oproj(const void* attn_out, const void* w_o, const 
  *     requests up to the last granted one. It equals n_free_out unless a
  *     request before that one was refused; then it is negative, and so many
  *     pages have to come free before the refused ones among them can run.
+ *     Requests refused after the last granted one do not enter it: a list
+ *     that runs out and stays out shows in granted alone.
  *   status: DEVICE int32 or NULL: FDLLM_ERR_DEVICE_BOUNDS is written there
  *     for a negative length, a request past its table's end (both get no
  *     rows and granted 0), a page id outside [0, num_pages) (its rows get
