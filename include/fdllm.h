@@ -349,8 +349,12 @@ FDLLM_API fdllm_status fdllm_oproj(const void* attn_out, const void* w_o, const 
  *     per row its position, the logical slot it writes (the position; -1 if
  *     refused), its request, and its place in the pool, page * page_size +
  *     offset (-1 if refused). positions, slots and block_table are the
- *     arguments of those names of fdllm_layer_step and
- *     fdllm_decode_attention. Entries past the last row stay as they are.
+ *     arguments of those names of fdllm_layer_step, which also wants host
+ *     copies of cu_rows and the lengths. Entries past the last row stay as
+ *     they are. The rows lie close together: a request without new tokens
+ *     (or past its table's end) has none, and the entries of those behind it
+ *     move up, so fdllm_decode_attention, which reads an entry a sequence,
+ *     takes the outputs of fdllm_plan_step.
  *   seq_lens_out int32 [batch], granted int32 [batch], n_free_out int32 [1].
  *   headroom int32 [1] or NULL: n_free less the pages asked for by all
  *     requests up to the last granted one. It equals n_free_out unless a
@@ -372,6 +376,25 @@ FDLLM_API fdllm_status fdllm_plan_blocks(int32_t batch, int32_t max_blocks_per_s
                                          int64_t* slot_map, int32_t* seq_lens_out,
                                          int32_t* granted, int32_t* n_free_out,
                                          int32_t* headroom, int32_t* status, void* stream);
+
+/* fdllm_plan_blocks with two outputs more, an entry a request, for
+ * fdllm_decode_attention over the same batch:
+ *   seq_positions, seq_slots: DEVICE int32 [batch] or NULL: position and
+ *     slot of the request's last row (its only one in a single-token step);
+ *     0 and -1 where it has no row or was refused, so that nothing is written
+ *     for it and its out means nothing.
+ * A request given several tokens belongs to the multi-row step: only its
+ * last one is named here. */
+FDLLM_API fdllm_status fdllm_plan_step(int32_t batch, int32_t max_blocks_per_seq,
+                                       int32_t page_size, int32_t num_pages, int32_t capacity,
+                                       const int32_t* seq_lens, const int32_t* new_lens,
+                                       int32_t* block_table, const int32_t* free_pages,
+                                       const int32_t* n_free, int32_t* cu_rows,
+                                       int32_t* positions, int32_t* slots, int32_t* row_seq,
+                                       int64_t* slot_map, int32_t* seq_lens_out,
+                                       int32_t* granted, int32_t* n_free_out,
+                                       int32_t* headroom, int32_t* seq_positions,
+                                       int32_t* seq_slots, int32_t* status, void* stream);
 
 /* Gives pages back: request b keeps its first keep_lens[b] tokens (all of
  * them when that is more than it holds; 0 ends it), and the pages past them
@@ -442,9 +465,9 @@ FDLLM_API int64_t fdllm_decode_workspace_bytes(int32_t n_heads, int32_t n_kv_hea
  *     q, k, v may be slices of one buffer; pointers and row strides (in
  *     bytes) are multiples of 16.
  *   positions: DEVICE int32 [batch]; needed with the RoPE tables, and with k
- *     when slots is NULL.
- *   slots: DEVICE int32 [batch], the slot the new k and v go to, or NULL:
- *     slot = position. A negative slot writes nothing. No two sequences may
+ *     when slots is NULL (seq_positions of fdllm_plan_step).
+ *   slots: DEVICE int32 [batch], the slot the new k and v go to (seq_slots of
+ *     fdllm_plan_step), or NULL: slot = position. A negative slot writes nothing. No two sequences may
  *     write one place of the pool, and none may see a slot that another
  *     sequence writes in this call.
  *   rope_cos, rope_sin: DEVICE fp64 [max_position][head_dim / 2], as for
@@ -559,7 +582,7 @@ FDLLM_API const char* fdllm_last_error(void);
 
 /* Number of kernel launches the last successful fdllm_layer_step,
  * fdllm_layer_step_noalloc, fdllm_select_tracked, fdllm_verify_accept,
- * fdllm_oproj, fdllm_plan_blocks, fdllm_release_blocks,
+ * fdllm_oproj, fdllm_plan_blocks, fdllm_plan_step, fdllm_release_blocks,
  * fdllm_decode_attention or fdllm_linear call on this thread enqueued. */
 FDLLM_API int32_t fdllm_last_launch_count(void);
 

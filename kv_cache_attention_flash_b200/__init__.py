@@ -253,7 +253,7 @@ def _native():
             raise ImportError("_serve.so is missing or does not load: build it with "
                               "`python -m kv_cache_attention_flash_b200.build`") from e
         _serve.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
-            "fdllm_plan_blocks", "fdllm_release_blocks", "fdllm_decode_workspace_bytes",
+            "fdllm_plan_step", "fdllm_release_blocks", "fdllm_decode_workspace_bytes",
             "fdllm_decode_attention", "fdllm_linear")))
         _bound = lib
     return _serve
@@ -291,7 +291,8 @@ def fdllm_plan_buffers(batch: int, capacity: int, device="cuda") -> dict:
             "slots": torch.empty(capacity, **i32), "row_seq": torch.empty(capacity, **i32),
             "slot_map": torch.empty(capacity, dtype=torch.int64, device=device),
             "seq_lens": torch.empty(batch, **i32), "granted": torch.empty(batch, **i32),
-            "n_free": torch.empty(1, **i32), "headroom": torch.empty(1, **i32)}
+            "n_free": torch.empty(1, **i32), "headroom": torch.empty(1, **i32),
+            "seq_positions": torch.empty(batch, **i32), "seq_slots": torch.empty(batch, **i32)}
 
 
 def fdllm_plan_blocks(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
@@ -301,9 +302,11 @@ def fdllm_plan_blocks(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_tabl
     """Block tables, positions and slot maps of a step, pages taken from the
     free list (see include/fdllm.h); block_table is updated in place.
 
-    out: buffers as fdllm_plan_buffers gives them ("headroom" may be left
-    out); without it, `capacity`
-    (room for the step's rows) is needed. Returns them."""
+    out: buffers as fdllm_plan_buffers gives them ("headroom", "seq_positions"
+    and "seq_slots" may be left out); without it, `capacity` (room for the
+    step's rows) is needed. Returns them. "positions" and "slots" have an entry
+    for each new row; for fdllm_decode_attention take "seq_positions" and
+    "seq_slots", which have one for each request, also for one without a row."""
     if stream is not None:
         with _on(stream, block_table):
             return fdllm_plan_blocks(seq_lens, new_lens, block_table, page_size, free_pages, n_free,
@@ -367,7 +370,8 @@ def fdllm_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.
 
     q: [B, n_heads * D]; k, v: [B, n_kv_heads * D] (rows may be strided, so
     that the three can be slices of one projection). The pools give the
-    layout [n_layers, num_pages, n_kv_heads, page_size, D]. scale: default
+    layout [n_layers, num_pages, n_kv_heads, page_size, D]. positions, slots:
+    [B], "seq_positions" and "seq_slots" of fdllm_plan_blocks. scale: default
     1 / sqrt(D). Returns (out [B, n_heads * D], lse [B, n_heads] or None).
     workspace: a uint8 tensor of fdllm_decode_workspace_bytes, else one is
     allocated for the call."""

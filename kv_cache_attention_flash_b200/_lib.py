@@ -74,6 +74,7 @@ SIGNATURES = {
     "fdllm_plan_tile_schedule": (_i32, [_vp, _i32, _i32, _i32, _vp, _vp]),
     "fdllm_oproj": (_i32, [_vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp]),
     "fdllm_plan_blocks": (_i32, [_i32] * 5 + [_vp] * 16),
+    "fdllm_plan_step": (_i32, [_i32] * 5 + [_vp] * 18),
     "fdllm_release_blocks": (_i32, [_i32] * 4 + [_vp] * 9),
     "fdllm_decode_workspace_bytes": (ctypes.c_int64, [_i32, _i32, _i32]),
     "fdllm_decode_attention": (_i32, [ctypes.POINTER(Decode), _i32] + [_vp] * 15 +

@@ -20,7 +20,7 @@
 
 namespace {
 
-decltype(&fdllm_plan_blocks) plan_blocks_fn = nullptr;
+decltype(&fdllm_plan_step) plan_step_fn = nullptr;
 decltype(&fdllm_release_blocks) release_blocks_fn = nullptr;
 decltype(&fdllm_decode_workspace_bytes) workspace_fn = nullptr;
 decltype(&fdllm_decode_attention) decode_fn = nullptr;
@@ -140,8 +140,11 @@ PyObject* plan_blocks(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t np = free_pages.numel();
   PyObject* pos = item(a[6], "positions");
   const int64_t cap = needed(pos, "positions").numel();
-  PyObject* headroom = PyDict_GetItemString(a[6], "headroom");   // may be left out
-  return result(plan_blocks_fn(
+  auto wanted = [&](const char* name, int64_t size) {             // may be left out
+    PyObject* o = PyDict_GetItemString(a[6], name);
+    return call.i32<int32_t>(o ? o : Py_None, name, {size});
+  };
+  return result(plan_step_fn(
       as_int(B, "batch"), as_int(mb, "block_table's width"), as_int(a[3], "page_size"),
       as_int(np, "free_pages"), as_int(cap, "capacity"), call.i32<int32_t>(a[0], "seq_lens", {B}),
       call.i32<int32_t>(a[1], "new_lens", {B}), call.i32<int32_t>(a[2], "block_table", {B, mb}),
@@ -155,7 +158,7 @@ PyObject* plan_blocks(PyObject*, PyObject* const* a, Py_ssize_t n) {
       call.i32<int32_t>(item(a[6], "seq_lens"), "seq_lens (out)", {B}),
       call.i32<int32_t>(item(a[6], "granted"), "granted", {B}),
       call.i32<int32_t>(item(a[6], "n_free"), "n_free (out)", {1}),
-      call.i32<int32_t>(headroom ? headroom : Py_None, "headroom", {1}),
+      wanted("headroom", 1), wanted("seq_positions", B), wanted("seq_slots", B),
       call.i32<int32_t>(a[7], "status", {1}), call.stream()));
   END_HANDLE_TH_ERRORS
 }
@@ -311,7 +314,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p[i] = PyLong_AsVoidPtr(a[i]);
     if (PyErr_Occurred()) throw python_error();
   }
-  plan_blocks_fn = reinterpret_cast<decltype(plan_blocks_fn)>(p[0]);
+  plan_step_fn = reinterpret_cast<decltype(plan_step_fn)>(p[0]);
   release_blocks_fn = reinterpret_cast<decltype(release_blocks_fn)>(p[1]);
   workspace_fn = reinterpret_cast<decltype(workspace_fn)>(p[2]);
   decode_fn = reinterpret_cast<decltype(decode_fn)>(p[3]);

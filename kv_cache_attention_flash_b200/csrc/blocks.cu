@@ -149,6 +149,9 @@ __global__ void __launch_bounds__(PT, 6) plan_kernel(const PlanArgs a) {
       a.cu_rows[b] = row0;
       a.seq_lens_out[b] = ok ? r.len + r.rows : a.seq_lens[b];
       a.granted[b] = ok ? 1 : 0;
+      const bool row = ok && r.rows > 0;
+      if (a.seq_positions) a.seq_positions[b] = row ? r.len + r.rows - 1 : 0;
+      if (a.seq_slots) a.seq_slots[b] = row ? r.len + r.rows - 1 : -1;
       if (r.bad) report(a.status);
     }
   }

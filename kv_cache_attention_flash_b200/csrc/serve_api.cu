@@ -65,6 +65,20 @@ fdllm_status fdllm_plan_blocks(int32_t batch, int32_t max_blocks, int32_t page_s
                                int32_t* positions, int32_t* slots, int32_t* row_seq,
                                int64_t* slot_map, int32_t* seq_lens_out, int32_t* granted,
                                int32_t* n_free_out, int32_t* headroom, int32_t* status, void* stream) {
+  return fdllm_plan_step(batch, max_blocks, page_size, num_pages, capacity, seq_lens, new_lens,
+                         block_table, free_pages, n_free, cu_rows, positions, slots, row_seq,
+                         slot_map, seq_lens_out, granted, n_free_out, headroom, nullptr, nullptr,
+                         status, stream);
+}
+
+fdllm_status fdllm_plan_step(int32_t batch, int32_t max_blocks, int32_t page_size,
+                             int32_t num_pages, int32_t capacity, const int32_t* seq_lens,
+                             const int32_t* new_lens, int32_t* block_table,
+                             const int32_t* free_pages, const int32_t* n_free, int32_t* cu_rows,
+                             int32_t* positions, int32_t* slots, int32_t* row_seq,
+                             int64_t* slot_map, int32_t* seq_lens_out, int32_t* granted,
+                             int32_t* n_free_out, int32_t* headroom, int32_t* seq_positions,
+                             int32_t* seq_slots, int32_t* status, void* stream) {
   NvtxRange nvtx_range("fdllm_plan_blocks");
   fdllm_status st = check_plan("plan_blocks", batch, max_blocks, page_size, num_pages);
   if (st != FDLLM_OK) return st;
@@ -78,7 +92,8 @@ fdllm_status fdllm_plan_blocks(int32_t batch, int32_t max_blocks, int32_t page_s
   const uint64_t nb = (uint64_t)batch * 4, nc = (uint64_t)capacity * 4;
   const Span outs[] = {{block_table, nb * max_blocks}, {cu_rows, nb + 4}, {positions, nc},
                        {slots, nc}, {row_seq, nc}, {slot_map, 2 * nc}, {seq_lens_out, nb},
-                       {granted, nb}, {n_free_out, 4}, {headroom, 4}};
+                       {granted, nb}, {n_free_out, 4}, {headroom, 4}, {seq_positions, nb},
+                       {seq_slots, nb}};
   const Span ins[] = {{seq_lens, nb}, {new_lens, nb}, {free_pages, (uint64_t)num_pages * 4},
                       {n_free, 4}, {status, 4}};
   for (const Span& s : outs)
@@ -108,6 +123,8 @@ fdllm_status fdllm_plan_blocks(int32_t batch, int32_t max_blocks, int32_t page_s
   a.granted = granted;
   a.n_free_out = n_free_out;
   a.headroom = headroom;
+  a.seq_positions = seq_positions;
+  a.seq_slots = seq_slots;
   a.status = status;
   a.vec = aligned(positions, 16) && aligned(slots, 16) && aligned(row_seq, 16) &&
           aligned(slot_map, 16);

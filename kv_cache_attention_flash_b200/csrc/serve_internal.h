@@ -76,6 +76,8 @@ struct PlanArgs {
   int32_t* granted;
   int32_t* n_free_out;
   int32_t* headroom;          // null: not wanted
+  int32_t* seq_positions;     // and these
+  int32_t* seq_slots;
   int32_t* status;
   int vec;                    // the row outputs are 16-byte aligned
 };

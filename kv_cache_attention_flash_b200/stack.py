@@ -99,8 +99,10 @@ class LayerStack:
                stream=None, outs=None) -> torch.Tensor:
         """One new token a sequence through the stack: x bf16 [B, H], the
         token's position, the slot its k and v go to (default: the position)
-        and the slots it sees, itself included (device int32 [B] each;
-        fdllm_plan_blocks gives them with the block table). The residual
+        and the slots it sees, itself included (device int32 [B] each:
+        "seq_positions", "seq_slots" and "seq_lens" of fdllm_plan_blocks, not
+        its row outputs, whose entries move up where a request has no row; a
+        request without a row writes nothing and its x means nothing). The residual
         stream ends in x_out (default: x). A call may be captured after a
         first one outside a capture has built the cache's RoPE tables. `outs`,
         a dict, receives each layer's intermediate results (for tests)."""
