@@ -489,7 +489,9 @@ FDLLM_API int64_t fdllm_decode_workspace_bytes(int32_t n_heads, int32_t n_kv_hea
  *     for a length outside [0, max_blocks_per_seq * page_size], a position
  *     outside the tables or a slot past the block table (such a sequence
  *     writes nothing and its out is zero), and for a page id outside
- *     [0, num_pages) (its slots are left out).
+ *     [0, num_pages) (its slots are left out); FDLLM_ERR_TIMEOUT when a
+ *     bounded in-kernel wait gives up (out and lse are then incomplete).
+ *     Nothing else writes it. Without it such errors are not reported.
  * Sums and softmax statistics are fp32. With a bf16 pool q' and the
  * probabilities enter the products as pairs of bf16 (16 bits). Results do
  * not depend on the order in which the GPU runs the CTAs. Two launches. */

@@ -444,6 +444,8 @@ class FlashCache:
         self.max_position = max_position
         self.rope_theta = rope_theta
         self._rope = None
+        # what decode() meets on the device, for check()
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.k_pool.device)
         self.handle = fdllm_cache_create(n_layers, n_heads, head_dim, page_size, num_pages,
                                          max_position, rope_theta, dtype, self.k_pool, self.v_pool,
                                          max_batch, max_slots_per_seq)
@@ -472,14 +474,28 @@ class FlashCache:
                out=None, out_dtype=torch.float32, lse=None, with_lse=False, workspace=None,
                status=None, stream=None):
         """One new token a sequence: RoPE, the write of k and v, attention
-        over the visible slots (fdllm_decode_attention on this cache)."""
+        over the visible slots (fdllm_decode_attention on this cache).
+        Device-side errors are raised by the next check(), or written to
+        `status` alone when that is given."""
+        status = self.status if status is None else status
         cos, sin = self.rope_tables()
         return fdllm_decode_attention(q, self.k_pool, self.v_pool, layer, block_table, seq_lens, k,
                                       v, positions, slots, cos, sin, starts, None, out, out_dtype,
                                       lse, with_lse, workspace, status, stream)
 
     def check(self, stream=None):
+        """Synchronises the stream and raises FdllmError on an error that a
+        step, or a decode() without a status of its own, met on the device
+        since the last check."""
         fdllm_check(self.handle, stream)
+        if stream is None:
+            code = int(self.status.item())
+            if code:
+                self.status.zero_()
+                raise FdllmError(code, load().fdllm_status_string(code).decode())
+        else:
+            with _on(stream, self.status):
+                self.check()
 
     def close(self):
         if self.handle:

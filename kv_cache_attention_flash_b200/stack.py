@@ -74,14 +74,15 @@ class LayerStack:
             n += fdllm_last_launch_count()
             if outs is not None:
                 outs[l] = self._out.clone()
-            fdllm_oproj(self._out, self.w_o[l], y=dst, residual=cur, stream=stream)
+            fdllm_oproj(self._out, self.w_o[l], y=dst, residual=cur, stream=stream,
+                        status=self.cache.status)
             n += fdllm_last_launch_count()
-            n += self._feed_forward(l, dst, stream)
+            n += self._feed_forward(l, dst, stream, self.cache.status)
             cur = dst
         self.launches = n
         return dst, attn_mass
 
-    def _feed_forward(self, l: int, x: torch.Tensor, stream, status=None, outs=None) -> int:
+    def _feed_forward(self, l: int, x: torch.Tensor, stream, status, outs=None) -> int:
         """x += (silu(x W_gate) * (x W_up)) W_down in place; launches made."""
         if self.mlp is None:
             return 0
@@ -104,12 +105,15 @@ class LayerStack:
         its row outputs, whose entries move up where a request has no row; a
         request without a row writes nothing and its x means nothing). The residual
         stream ends in x_out (default: x). A call may be captured after a
-        first one outside a capture has built the cache's RoPE tables. `outs`,
-        a dict, receives each layer's intermediate results (for tests)."""
+        first one outside a capture has built the cache's RoPE tables. Device-
+        side errors are raised by the cache's next check(), or written to
+        `status` alone when that is given. `outs`, a dict, receives each
+        layer's intermediate results (for tests)."""
         if stream is not None:
             with _on(stream, x):
                 return self.decode(x, positions, block_table, seq_lens, slots, x_out, status, None,
                                    outs)
+        status = self.cache.status if status is None else status
         H = x.shape[1]
         n = 0
         cur = x
