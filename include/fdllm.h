@@ -494,7 +494,9 @@ FDLLM_API int64_t fdllm_decode_workspace_bytes(int32_t n_heads, int32_t n_kv_hea
  *     Nothing else writes it. Without it such errors are not reported.
  * Sums and softmax statistics are fp32. With a bf16 pool q' and the
  * probabilities enter the products as pairs of bf16 (16 bits). Results do
- * not depend on the order in which the GPU runs the CTAs. Two launches. */
+ * not depend on the order in which the GPU runs the CTAs. A NaN score makes
+ * that head's out and lse NaN; so may an infinite k or v in a visible slot,
+ * whose product with the low half of a pair is one. Two launches. */
 FDLLM_API fdllm_status fdllm_decode_attention(
     const fdllm_decode* shape, int32_t layer, const void* q, const void* k, const void* v,
     const int32_t* positions, const int32_t* slots, const double* rope_cos,

@@ -290,6 +290,12 @@ __device__ __forceinline__ void write_out2(const DecodeArgs& a, int64_t at, floa
 
 __device__ __forceinline__ float inverse(float l) { return l > 0.f ? 1.f / l : (l == l ? 0.f : l); }
 
+// m: the largest score in steps of log2. Nothing seen: l = 0 and -inf. A NaN
+// score leaves m as it is (-inf when every score is one) and l NaN, which stays.
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l == 0.f ? -INFINITY : fmaf(m, kLn2, logf(l));
+}
+
 // Floats of a partial result: O of each head, then m, then l, each 16-byte
 // aligned as a whole.
 __host__ __device__ constexpr int part_floats(int heads, int head_dim) {
@@ -943,12 +949,11 @@ __global__ void __launch_bounds__(32 * (WARPS + loaders(kRows)), 2) decode_kerne
         if (flags & kWhole) {
           const float inv = inverse(l);
           write_out2(a, (head0 + h) * D + d, x * inv, y * inv);
-          if (d == 0 && a.lse)
-            a.lse[head0 + h] = m == -INFINITY ? -INFINITY : m * c * kLn2 + logf(l);
+          if (d == 0 && a.lse) a.lse[head0 + h] = lse_of(m * c, l);
         } else {
           *reinterpret_cast<float2*>(part + h * D + d) = make_float2(x, y);
           if (d == 0) {
-            part[a.unit_heads * D + h] = m == -INFINITY ? -INFINITY : m * c;
+            part[a.unit_heads * D + h] = m * c;
             part[a.unit_heads * (D + 1) + h] = l;
           }
         }
@@ -1034,8 +1039,10 @@ __global__ void __launch_bounds__(JT) join_kernel(const DecodeArgs a) {
     x.x *= f, x.y *= f, x.z *= f, x.w *= f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      if (pm[i] != -INFINITY) {         // (an empty part adds nothing)
-        const float fi = ptx::ex2(pm[i] - mn);
+      if (c + i * JW <= c1) {
+        // (an empty part adds zeros; one whose scores are all NaN has no maximum
+        // either, and its NaN stays)
+        const float fi = pm[i] == -INFINITY ? 0.f : ptx::ex2(pm[i] - mn);
         l = fmaf(fi, pl[i], l);
         add(fi, px[i]);
       }
@@ -1066,7 +1073,7 @@ __global__ void __launch_bounds__(JT) join_kernel(const DecodeArgs a) {
     write_out2(a, q_head * D + lane * 4, x.x * inv, x.y * inv);
     write_out2(a, q_head * D + lane * 4 + 2, x.z * inv, x.w * inv);
   }
-  if (lane == 0 && a.lse) a.lse[q_head] = m == -INFINITY ? -INFINITY : m * kLn2 + logf(l);
+  if (lane == 0 && a.lse) a.lse[q_head] = lse_of(m, l);
 }
 
 // The layer's slice of a pool in 4 dimensions (element of a piece, row of a
