@@ -22,7 +22,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libfdllm.so")
 SOURCES = ["api.cu", "step_bf16.cu", "step_f32.cu", "mass_select.cu", "verify.cu", "oproj.cu",
            "serve_api.cu", "blocks.cu", "decode_attn.cu", "linear.cu"]
-HEADERS = ["fdllm_internal.h", "host_api.h", "ptx.cuh", "ptx_serve.cuh", "serve_internal.h"]
+HEADERS = ["fdllm_internal.h", "host_api.h", "ptx.cuh", "ptx_serve.cuh", "serve_index.h", "serve_internal.h"]
 
 EXT = os.path.join(PKG, "_serve.so")
 EXT_SRC = os.path.join(CSRC, "bind.cpp")

@@ -60,6 +60,7 @@
 #include "fdllm_internal.h"
 #include "host_api.h"
 #include "ptx_serve.cuh"
+#include "serve_index.h"
 #include "serve_internal.h"
 
 namespace fdllm {
@@ -780,8 +781,9 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, const CUtensorMa
       at.next_unit(a);
     }
     if (!asked) break;
-    // (a wait that gives up ends the work, and is reported)
-    ok = ok && __all_sync(0xffffffffu, wait_arrival(&ctrl.took, answers & 1, a.status));
+    // (a wait that gives up ends the work, and is reported; the answer is waited
+    // for all the same, it comes into this CTA's memory)
+    ok = __all_sync(0xffffffffu, wait_arrival(&ctrl.took, answers & 1, a.status)) && ok;
     ++answers;
     share = ok ? ptx::taken_cta(ctrl.answer) : -1;
     // every loading warp has read the answer before the next request
@@ -790,14 +792,20 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, const CUtensorMa
     if (share < 0) break;
   }
   wait_empty();
-  if (lane == 0 && first) ctrl.tile[stage].flags = kStop;
-  __syncwarp();
-  ptx::cp_async_arrive(&ctrl.full[stage]);
-  // what was loaded has been consumed when the computing warps have left, or
-  // has arrived here
-  for (int i = 1; i < S::STAGES; ++i)
-    if (!ok) wait_arrival(&ctrl.full[(stage + i) % S::STAGES], round & 1, nullptr);
+  if (ok) {
+    if (lane == 0 && first) ctrl.tile[stage].flags = kStop;
+    __syncwarp();
+    ptx::cp_async_arrive(&ctrl.full[stage]);
+  }
+  // No copy is under way when this warp leaves: the computing warps may have given
+  // up before it. (After a wait that gave up here the next stage may hold one too.)
   ptx::cp_async_wait_all();
+  if (lane != 0) return;
+#pragma unroll 1
+  for (int s = 0; s < S::STAGES; ++s) {
+    const int pass = last_pass(s, stage, (int)round);
+    if (pass >= 0 && !(ok && s == stage)) wait_arrival(&ctrl.full[s], pass & 1, nullptr);
+  }
 }
 
 template <bool kF32, int D, int HT, bool kRows>
