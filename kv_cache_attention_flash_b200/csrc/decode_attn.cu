@@ -185,7 +185,7 @@ constexpr int kStop = 64;               // no tile: the work is done
 
 template <int STAGES>
 struct Ctrl {
-  uint64_t full[STAGES];                // a tile has come: 32 arrivals of the loading warp
+  uint64_t full[STAGES];                // a tile has come: 33 arrivals of a loading warp
   uint64_t empty[STAGES];               // it is consumed: one arrival a warp
   uint64_t took;                        // the answer in `answer` has arrived
   uint64_t met;                         // the computing warps meet, and
@@ -606,6 +606,15 @@ __device__ __forceinline__ bool meet(uint64_t* bar, uint32_t& phase, int32_t* st
   return ok;
 }
 
+// The arrivals of a loading warp at a stage's barrier: each lane's once its
+// copies are there, and one that releases what the warp has stored for the tile
+// (an arrival that waits for copies orders copies, not stores).
+__device__ __forceinline__ void publish(uint64_t* full) {
+  ptx::cp_async_arrive(full);
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(full);
+}
+
 // A loading warp: walks the shares, brings every tile (by rows: its quarter of
 // it) and, the first of them, the unit's q.
 template <bool kF32, int D, bool kRows>
@@ -772,7 +781,7 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, const CUtensorMa
           tile->key0 = key0;
           tile->part = 2 * share + (first_segment ? 0 : 1);
         }
-        ptx::cp_async_arrive(bar);
+        publish(bar);
         flags &= ~(kFirst | kRow);
         next_stage();
       }
@@ -794,8 +803,7 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, const CUtensorMa
   wait_empty();
   if (ok) {
     if (lane == 0 && first) ctrl.tile[stage].flags = kStop;
-    __syncwarp();
-    ptx::cp_async_arrive(&ctrl.full[stage]);
+    publish(&ctrl.full[stage]);
   }
   // No copy is under way when this warp leaves: the computing warps may have given
   // up before it. (After a wait that gave up here the next stage may hold one too.)
@@ -828,7 +836,7 @@ __global__ void __launch_bounds__(32 * (WARPS + loaders(kRows)), 2) decode_kerne
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < S::STAGES; ++i) {
-      ptx::mbar_init(&ctrl.full[i], 32 * loaders(kRows));
+      ptx::mbar_init(&ctrl.full[i], 33 * loaders(kRows));
       ptx::mbar_init(&ctrl.empty[i], WARPS);
     }
     ptx::mbar_init(&ctrl.took, 1);
