@@ -183,6 +183,14 @@ constexpr int kNew = 16;                // and is one of this tile's
 constexpr int kBad = 32;                // the sequence's metadata is out of range
 constexpr int kStop = 64;               // no tile: the work is done
 
+// The joining launch starts under the first one's tail, and reads the lengths
+// (for which parts there are) while it waits. Its own wait would make them
+// visible, but ends with the first launch. So one thread of the first launch,
+// past its wait for what came before, releases this mark, and a joining warp that
+// acquires it may read on; one that does not find it waits first. The joining
+// launch takes the mark off again. (1 x 768: 8.5 us; 9.7 with the wait first.)
+constexpr unsigned long long kBegun = 0x64c0de5eb8f3a127ull;
+
 template <int STAGES>
 struct Ctrl {
   uint64_t full[STAGES];                // a tile has come: 33 arrivals of a loading warp
@@ -856,6 +864,7 @@ __global__ void __launch_bounds__(32 * (WARPS + loaders(kRows)), 2) decode_kerne
     load_tiles<kF32, D, kRows>(a, &tmap_k, &tmap_v, ctrl, ring, slots);
     return;
   }
+  if (blockIdx.x == 0 && tid == 0) ptx::st_release_gpu(a.begun, kBegun);
 
   const float c = a.scale * kLog2e;
   float* my_ps = kF32 ? ps + warp * S::KS * HT : ps;
@@ -1000,8 +1009,7 @@ __global__ void __launch_bounds__(JT) join_kernel(const DecodeArgs a) {
   const int b = real ? (int)(q_head / a.n_heads) : 0, head = (int)(q_head - (int64_t)b * a.n_heads);
   const int hk = head / a.group, g = head - hk * a.group;
   const int u = hk * a.head_chunks + g / NH, h = g % NH;
-  // (the line is read before the wait: it is older than the launch that
-  // leaves the parts)
+  if (__any_sync(0xffffffffu, ptx::ld_acquire_gpu(a.begun) != kBegun)) ptx::wait_primary();
   int before = 0;
   Window<S::TILE> line;
   line.read(a, 0, 0);
@@ -1021,6 +1029,7 @@ __global__ void __launch_bounds__(JT) join_kernel(const DecodeArgs a) {
   const bool at_front = shares.begin(c0) == t0;
   ptx::wait_primary();
   ptx::launch_dependents();
+  if (blockIdx.x == 0 && tid == 0) *a.begun = 0;
   if (!real || c0 == c1) return;        // JW > 1: the same for the whole CTA
   auto part = [&](int c) {
     return a.part + (int64_t)(2 * c + (c == c0 && !at_front ? 1 : 0)) * part_floats(a.unit_heads, D);
@@ -1189,7 +1198,7 @@ int decode_ctas(int sms) { return 8 * sms; }
 
 size_t decode_workspace_bytes(int group, int head_dim, int sms) {
   const int heads = group < NH ? group : NH;
-  return (size_t)decode_ctas(sms) * 2 * part_floats(heads, head_dim) * sizeof(float);
+  return (size_t)decode_ctas(sms) * 2 * part_floats(heads, head_dim) * sizeof(float) + 16;
 }
 
 cudaError_t launch_decode_attention(const DecodeArgs& a, int head_dim, bool f32, int sms,

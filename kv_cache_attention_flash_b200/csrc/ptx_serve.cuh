@@ -81,6 +81,18 @@ __device__ __forceinline__ void wait_primary() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// A store that releases what this thread knows of (its own writes, and those
+// that its waits made visible to it) to an acquiring load anywhere on the GPU.
+__device__ __forceinline__ void st_release_gpu(unsigned long long* p, unsigned long long v) {
+  asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
+}
+
+__device__ __forceinline__ unsigned long long ld_acquire_gpu(const unsigned long long* p) {
+  unsigned long long v;
+  asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+  return v;
+}
+
 __device__ __forceinline__ void tma_load_4d_at(uint32_t dst, const CUtensorMap* map, int c0, int c1,
                                                int c2, int c3, uint64_t* bar) {
   asm volatile(

@@ -274,6 +274,7 @@ fdllm_status fdllm_decode_attention(const fdllm_decode* d, int32_t layer, const 
   a.out = out;
   a.lse = lse;
   a.part = reinterpret_cast<float*>(workspace);
+  a.begun = reinterpret_cast<unsigned long long*>(reinterpret_cast<uint8_t*>(workspace) + need - 16);
   a.status = status;
   a.batch = d->batch;
   a.n_heads = d->n_heads;

@@ -104,6 +104,7 @@ struct DecodeArgs {
   void* out;
   float* lse;                 // null: not wanted
   float* part;                // workspace
+  unsigned long long* begun;  // behind the parts (see kBegun)
   int32_t* status;
   int batch, n_heads, n_kv_heads, group, head_chunks, units_per_seq;
   int max_blocks, num_pages, max_position, in_f32, out_bf16;
