@@ -379,6 +379,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
   }
   ptx::tc_fence_before();
   __syncthreads();
+  // the even CTA's last arrival at the odd one's barriers, behind all the others
+  if (warp == 1 && rank == 1) wait_for(&ctrl.drained, 0);
   ptx::cluster_sync_warps();                   // the peer's loads, arrivals and products are done too
   ptx::tc_fence_after();
   if (warp == 1) ptx::tmem_dealloc_pair(tmem, 2 * W_COLS);
