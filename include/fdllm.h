@@ -578,6 +578,15 @@ FDLLM_API fdllm_status fdllm_check(fdllm_cache* cache, void* stream);
 typedef enum { FDLLM_INJECT_NONE = 0, FDLLM_INJECT_SPLIT_FLAG_TIMEOUT = 1 } fdllm_inject_kind;
 FDLLM_API fdllm_status fdllm_inject_fault(fdllm_cache* cache, int32_t kind, int64_t wait_ns);
 
+/* The same for the single-token calls, which have no handle: the next
+ * fdllm_decode_attention or fdllm_linear of this thread that enqueues work
+ * says of the first tile of every CTA that it is not there (its copies are
+ * made and waited for), and bounds its waits to about wait_ns nanoseconds
+ * (1 .. 1e9) instead of a second. They run out, FDLLM_ERR_TIMEOUT is written to
+ * that call's status, and its output is incomplete (k and v may not be in the
+ * cache). Applies once; 0 cancels it. */
+FDLLM_API fdllm_status fdllm_inject_tile_timeout(int64_t wait_ns);
+
 /* Static description of a status code. */
 FDLLM_API const char* fdllm_status_string(fdllm_status status);
 

@@ -28,7 +28,7 @@ __all__ = [
     "fdllm_select_tracked", "fdllm_verify_accept", "fdllm_plan_tile_schedule", "fdllm_oproj",
     "fdllm_plan_blocks", "fdllm_release_blocks", "fdllm_plan_buffers", "fdllm_decode_attention",
     "fdllm_rope_tables", "fdllm_linear",
-    "fdllm_check", "fdllm_inject_fault", "fdllm_last_launch_count", "FlashCache", "FdllmError",
+    "fdllm_check", "fdllm_inject_fault", "fdllm_inject_tile_timeout", "fdllm_last_launch_count", "FlashCache", "FdllmError",
     "load",
 ]
 
@@ -421,6 +421,12 @@ def fdllm_inject_fault(handle: int, kind: int, wait_ns: int = 0) -> None:
     include/fdllm.h: the attending CTAs' bounded flag wait runs out after
     wait_ns and the step records FDLLM_ERR_TIMEOUT)."""
     check_status(load().fdllm_inject_fault(handle, int(kind), int(wait_ns)))
+
+
+def fdllm_inject_tile_timeout(wait_ns: int = 0) -> None:
+    """Makes the waits of this thread's next fdllm_decode_attention or
+    fdllm_linear run out after wait_ns (see include/fdllm.h); 0 cancels it."""
+    check_status(load().fdllm_inject_tile_timeout(int(wait_ns)))
 
 
 def fdllm_last_launch_count() -> int:

@@ -82,6 +82,7 @@ SIGNATURES = {
     "fdllm_linear": (_i32, [ctypes.POINTER(LinearShape)] + [_vp] * 9),
     "fdllm_check": (_i32, [_vp, _vp]),
     "fdllm_inject_fault": (_i32, [_vp, _i32, ctypes.c_int64]),
+    "fdllm_inject_tile_timeout": (_i32, [ctypes.c_int64]),
     "fdllm_status_string": (ctypes.c_char_p, [_i32]),
     "fdllm_last_error": (ctypes.c_char_p, []),
     "fdllm_last_launch_count": (_i32, []),

@@ -591,13 +591,15 @@ struct Warp<true, D, HT> {
 };
 
 // ---------------------------------------------------------------- the shares
-// Waits for an arrival, for a second at most.
-__device__ __forceinline__ bool wait_arrival(uint64_t* bar, uint32_t parity, int32_t* status) {
+// Waits for an arrival, for a second at most; reported if `said`.
+__device__ __forceinline__ bool wait_arrival(uint64_t* bar, uint32_t parity, const DecodeArgs& a,
+                                             bool said = true) {
   if (ptx::mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   while (!ptx::mbar_try_wait(bar, parity))
-    if (clock64() - t0 > 2000000000ll) {
-      if (status) atomicExch(reinterpret_cast<int*>(status), (int)FDLLM_ERR_TIMEOUT);
+    if (clock64() - t0 > a.wait_cycles) {
+      if (said && a.status)
+        atomicExch(reinterpret_cast<int*>(a.status), (int)FDLLM_ERR_TIMEOUT);
       return false;
     }
   return true;
@@ -605,10 +607,10 @@ __device__ __forceinline__ bool wait_arrival(uint64_t* bar, uint32_t parity, int
 
 // Warps meet at `bar` (its count is theirs); bounded as every wait here, so
 // that none is held up by another that gave up.
-__device__ __forceinline__ bool meet(uint64_t* bar, uint32_t& phase, int32_t* status) {
+__device__ __forceinline__ bool meet(uint64_t* bar, uint32_t& phase, const DecodeArgs& a) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(bar);
-  const bool ok = __all_sync(0xffffffffu, wait_arrival(bar, phase & 1, status));
+  const bool ok = __all_sync(0xffffffffu, wait_arrival(bar, phase & 1, a));
   ++phase;
   __syncwarp();
   return ok;
@@ -617,10 +619,10 @@ __device__ __forceinline__ bool meet(uint64_t* bar, uint32_t& phase, int32_t* st
 // The arrivals of a loading warp at a stage's barrier: each lane's once its
 // copies are there, and one that releases what the warp has stored for the tile
 // (an arrival that waits for copies orders copies, not stores).
-__device__ __forceinline__ void publish(uint64_t* full) {
+__device__ __forceinline__ void publish(uint64_t* full, bool withhold = false) {
   ptx::cp_async_arrive(full);
   __syncwarp();
-  if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(full);
+  if ((threadIdx.x & 31) == 0 && !withhold) ptx::mbar_arrive(full);
 }
 
 // A loading warp: walks the shares, brings every tile (by rows: its quarter of
@@ -653,7 +655,7 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, const CUtensorMa
   };
   auto wait_empty = [&] {
     if (round > 0 && ok)
-      ok = __all_sync(0xffffffffu, wait_arrival(&ctrl.empty[stage], (round - 1) & 1, a.status));
+      ok = __all_sync(0xffffffffu, wait_arrival(&ctrl.empty[stage], (round - 1) & 1, a));
     __syncwarp();
   };
   while (ok && shares.begin(share) < total) {
@@ -789,7 +791,8 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, const CUtensorMa
           tile->key0 = key0;
           tile->part = 2 * share + (first_segment ? 0 : 1);
         }
-        publish(bar);
+        // (withheld where a test wants the wait for it to run out: fdllm_inject_tile_timeout)
+        publish(bar, a.withhold && round == 0 && stage == 0);
         flags &= ~(kFirst | kRow);
         next_stage();
       }
@@ -800,11 +803,11 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, const CUtensorMa
     if (!asked) break;
     // (a wait that gives up ends the work, and is reported; the answer is waited
     // for all the same, it comes into this CTA's memory)
-    ok = __all_sync(0xffffffffu, wait_arrival(&ctrl.took, answers & 1, a.status)) && ok;
+    ok = __all_sync(0xffffffffu, wait_arrival(&ctrl.took, answers & 1, a)) && ok;
     ++answers;
     share = ok ? ptx::taken_cta(ctrl.answer) : -1;
     // every loading warp has read the answer before the next request
-    if (kRows) ok = meet(&ctrl.met_loaders, meetings, a.status) && ok;
+    if (kRows) ok = meet(&ctrl.met_loaders, meetings, a) && ok;
     else __syncwarp();
     if (share < 0) break;
   }
@@ -820,7 +823,7 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, const CUtensorMa
 #pragma unroll 1
   for (int s = 0; s < S::STAGES; ++s) {
     const int pass = last_pass(s, stage, (int)round);
-    if (pass >= 0 && !(ok && s == stage)) wait_arrival(&ctrl.full[s], pass & 1, nullptr);
+    if (pass >= 0 && !(ok && s == stage)) wait_arrival(&ctrl.full[s], pass & 1, a, false);
   }
 }
 
@@ -874,7 +877,7 @@ __global__ void __launch_bounds__(32 * (WARPS + loaders(kRows)), 2) decode_kerne
 #pragma unroll 1
   while (true) {
     // a tile that does not come within a second ends the work, reported
-    if (!__all_sync(0xffffffffu, wait_arrival(&ctrl.full[stage], phase, a.status))) break;
+    if (!__all_sync(0xffffffffu, wait_arrival(&ctrl.full[stage], phase, a))) break;
     __syncwarp();
     const Tile* tile = &ctrl.tile[stage];
     const int flags = tile->flags;
@@ -920,7 +923,7 @@ __global__ void __launch_bounds__(32 * (WARPS + loaders(kRows)), 2) decode_kerne
           vc[d + D / 2] = fresh[D + d + D / 2];
         }
       }
-      if (!meet(&ctrl.met, meetings, a.status)) break;
+      if (!meet(&ctrl.met, meetings, a)) break;
       w.open(qf, real);
     }
     bool wrote = false;                 // to the stage
@@ -952,7 +955,7 @@ __global__ void __launch_bounds__(32 * (WARPS + loaders(kRows)), 2) decode_kerne
       __syncwarp();
       w.close(reinterpret_cast<float*>(rows), ctrl.m[turn][warp], ctrl.l[turn][warp], heads);
       wrote = true;
-      if (!meet(&ctrl.met, meetings, a.status)) break;
+      if (!meet(&ctrl.met, meetings, a)) break;
       const int64_t head0 = (int64_t)tile->b * a.n_heads + tile->hk * a.group + tile->chunk * NH;
       float* part = a.part + (int64_t)tile->part * part_floats(a.unit_heads, D);
       const float* buf = reinterpret_cast<const float*>(ring + stage * S::STAGE);

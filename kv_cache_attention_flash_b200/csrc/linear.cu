@@ -50,7 +50,6 @@ namespace {
 
 constexpr int BK = 64;                   // depth of a stage: one 128-byte span
 constexpr int BOX = BK * 64 * 2;         // a box of W: 64 K rows x 64 columns, 8 KB
-constexpr long long WAIT_CYCLES = 2000000000ll;   // of the SM clock: about a second
 
 // ---------------------------------------------------------------- epilogue arithmetic
 __device__ __forceinline__ float activate(float x, int act) {
@@ -90,27 +89,35 @@ __device__ __forceinline__ float bias_at(const void* p, int i, int f32) {
 // A bounded wait without side effects, and one that marks the CTA and reports
 // when it (or another wait of the CTA) gives up. The producer and the issuer
 // pass here once a stage on one thread, so a completed barrier costs one probe.
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const LinearArgs& a) {
   if (ptx::mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   while (!ptx::mbar_try_wait(bar, parity))
-    if (clock64() - t0 > WAIT_CYCLES) return false;
+    if (clock64() - t0 > a.wait_cycles) return false;
   return true;
 }
 
 __device__ __forceinline__ bool lin_wait(int* abort, uint64_t* bar, uint32_t parity,
-                                         int32_t* status) {
+                                         const LinearArgs& a) {
   if (ptx::mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   while (!ptx::mbar_try_wait(bar, parity)) {
     if (*reinterpret_cast<volatile int*>(abort)) return false;
-    if (clock64() - t0 > WAIT_CYCLES) {
+    if (clock64() - t0 > a.wait_cycles) {
       atomicExch(abort, 1);
-      if (status) atomicExch(reinterpret_cast<int*>(status), (int)FDLLM_ERR_TIMEOUT);
+      if (a.status) atomicExch(reinterpret_cast<int*>(a.status), (int)FDLLM_ERR_TIMEOUT);
       return false;
     }
   }
   return true;
+}
+
+// Bytes to come for a stage, and the arrival that completes it with them (of the
+// first one withheld where a test wants its wait to run out: fdllm_inject_tile_timeout).
+__device__ __forceinline__ void expect(uint64_t* full, uint32_t bytes, bool first,
+                                       const LinearArgs& a) {
+  if (first && a.withhold) ptx::mbar_expect_tx(full, bytes);
+  else ptx::mbar_arrive_expect_tx(full, bytes);
 }
 
 // A place in a ring of stages; `parity` is that of its current pass.
@@ -208,12 +215,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
         const int row = m * 256 + (int)rank * 128;
         const int col = kGate ? n * 128 : n * 256 + (int)rank * 128;
         for (int k = 0; k < nkb * BK; k += BK, ++it, at.next(W_STAGES)) {
-          if (it >= W_STAGES && !lin_wait(&ctrl.abort, &ctrl.empty[at.s], at.parity ^ 1, a.status)) {
+          if (it >= W_STAGES && !lin_wait(&ctrl.abort, &ctrl.empty[at.s], at.parity ^ 1, a)) {
             ok = false;
             break;
           }
           const uint32_t st = ring + at.s * W_STAGE, bar = full0 + at.s * 8;
-          if (rank == 0) ptx::mbar_arrive_expect_tx(&ctrl.full[at.s], 2 * W_STAGE);
+          if (rank == 0) expect(&ctrl.full[at.s], 2 * W_STAGE, it == 0, a);
           ptx::tma_load_2d_pair(st, &tmap_x, k, row, bar);
           ptx::tma_load_2d_pair(st + 16384, tw, col, k, bar);
           ptx::tma_load_2d_pair(st + 16384 + BOX, tw, col + 64, k, bar);
@@ -223,7 +230,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
       // after a timeout
       if (rank == 0)
         for (int i = it > W_STAGES ? it - W_STAGES : 0; i < it; ++i)
-          wait_for(&ctrl.full[i % W_STAGES], (i / W_STAGES) & 1);
+          wait_for(&ctrl.full[i % W_STAGES], (i / W_STAGES) & 1, a);
     }
   } else if (warp == 1) {
     if (rank == 0 && ptx::elect_one()) {
@@ -237,11 +244,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
       bool ok = true;
       for (int t = blockIdx.x / 2; t < tiles && ok; t += pairs, ++i) {
         const int b = i & 1;
-        if (i >= 2 && !lin_wait(&ctrl.abort, &ctrl.acc_empty[b], ((i >> 1) - 1) & 1, a.status)) break;
+        if (i >= 2 && !lin_wait(&ctrl.abort, &ctrl.acc_empty[b], ((i >> 1) - 1) & 1, a)) break;
         ptx::tc_fence_after();
         const uint32_t acc = tmem + b * W_COLS;
         for (int kb = 0; kb < nkb; ++kb, at.next(W_STAGES)) {
-          if (!lin_wait(&ctrl.abort, &ctrl.full[at.s], at.parity, a.status)) {
+          if (!lin_wait(&ctrl.abort, &ctrl.full[at.s], at.parity, a)) {
             ok = false;
             break;
           }
@@ -257,7 +264,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
       }
       // no product is in flight when TMEM is freed
       ptx::umma_commit_pair(&ctrl.drained);
-      wait_for(&ctrl.drained, 0);
+      wait_for(&ctrl.drained, 0, a);
     }
   } else {
     // a warp: 32 rows (its TMEM lane quadrant) x half of the columns
@@ -286,7 +293,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
         }
       };
       if (a.residual) bring(0);
-      if (!__all_sync(0xffffffffu, lin_wait(&ctrl.abort, &ctrl.acc_full[b], (i >> 1) & 1, a.status)))
+      if (!__all_sync(0xffffffffu, lin_wait(&ctrl.abort, &ctrl.acc_full[b], (i >> 1) & 1, a)))
         break;
       ptx::tc_fence_after();
       const uint32_t acc = tmem + b * W_COLS + lane_base + half * (OUT_COLS / 2);
@@ -380,7 +387,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
   ptx::tc_fence_before();
   __syncthreads();
   // the even CTA's last arrival at the odd one's barriers, behind all the others
-  if (warp == 1 && rank == 1) wait_for(&ctrl.drained, 0);
+  if (warp == 1 && rank == 1) wait_for(&ctrl.drained, 0, a);
   ptx::cluster_sync_warps();                   // the peer's loads, arrivals and products are done too
   ptx::tc_fence_after();
   if (warp == 1) ptx::tmem_dealloc_pair(tmem, 2 * W_COLS);
@@ -481,11 +488,11 @@ __global__ void __launch_bounds__(N_THREADS, 1)
       int issued = 0, k = kb0 * BK;
       Ring at;
       for (; issued < nkb; ++issued, k += BK, at.next(stages)) {
-        if (issued >= stages && !lin_wait(&ctrl.abort, &ctrl.empty[at.s], at.parity ^ 1, a.status))
+        if (issued >= stages && !lin_wait(&ctrl.abort, &ctrl.empty[at.s], at.parity ^ 1, a))
           break;
         uint64_t* bar = &ctrl.full[at.s];
         const uint32_t st = ring + at.s * stage_bytes;
-        ptx::mbar_arrive_expect_tx(bar, bytes);
+        expect(bar, bytes, issued == 0, a);
         if (plan.blocked) {              // all boxes of a matrix in one copy
           ptx::tma_load_3d_at(st, &tmap_w, 0, k, n0 >> 6, bar);
           if (kGate) ptx::tma_load_3d_at(st + g_at, &tmap_g, 0, k, n0 >> 6, bar);
@@ -499,7 +506,7 @@ __global__ void __launch_bounds__(N_THREADS, 1)
       }
       // every copy has landed before the ring is reused, also after a timeout
       for (int kb = issued > stages ? issued - stages : 0; kb < issued; ++kb)
-        wait_for(&ctrl.full[kb % stages], (kb / stages) & 1);
+        wait_for(&ctrl.full[kb % stages], (kb / stages) & 1, a);
     }
   } else if (warp == 1) {
     if (ptx::elect_one()) {
@@ -508,7 +515,7 @@ __global__ void __launch_bounds__(N_THREADS, 1)
       const uint32_t ring = ptx::smem_u32(smem);
       Ring at;
       for (int kb = 0; kb < nkb; ++kb, at.next(stages)) {
-        if (!lin_wait(&ctrl.abort, &ctrl.full[at.s], at.parity, a.status)) break;
+        if (!lin_wait(&ctrl.abort, &ctrl.full[at.s], at.parity, a)) break;
         ptx::tc_fence_after();
         const uint32_t st = ring + at.s * stage_bytes;
         const uint64_t xd = ptx::desc_at(xh, st + x_at), wd = ptx::desc_at(wh, st);
@@ -534,7 +541,7 @@ __global__ void __launch_bounds__(N_THREADS, 1)
         ptx::umma_commit(&ctrl.empty[at.s]);
       }
       ptx::umma_commit(&ctrl.done);
-      wait_for(&ctrl.done, 0);   // no product is in flight when TMEM is freed
+      wait_for(&ctrl.done, 0, a);   // no product is in flight when TMEM is freed
     }
   } else {
     if (a.residual) {                    // this rank's rows are on the way when they are needed
@@ -544,7 +551,7 @@ __global__ void __launch_bounds__(N_THREADS, 1)
         ptx::prefetch_l2(reinterpret_cast<const __nv_bfloat16*>(a.residual) +
                          (int64_t)(m0 + r0 + i / lines) * a.ldr + n0 + i % lines * 64);
     }
-    lin_wait(&ctrl.abort, &ctrl.done, 0, a.status);
+    lin_wait(&ctrl.abort, &ctrl.done, 0, a);
     __syncwarp();
     ptx::tc_fence_after();
   }

@@ -37,6 +37,17 @@ bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(
 bool is_dtype(int32_t d) { return d == FDLLM_BF16 || d == FDLLM_F32; }
 uint64_t size_of(int32_t d) { return d == FDLLM_F32 ? 4 : 2; }
 
+// Set by fdllm_inject_tile_timeout for this thread's next call: the bound of the
+// waits in ns, 0: nothing.
+thread_local int64_t g_inject_wait_ns = 0;
+
+template <typename Args>
+void bound_waits(Args& a) {
+  a.withhold = g_inject_wait_ns > 0;
+  a.wait_cycles = g_inject_wait_ns > 0 ? 2 * g_inject_wait_ns : kWaitCycles;
+  g_inject_wait_ns = 0;
+}
+
 int sms_here() {
   const int n = sm_count();
   return n > 0 ? n : 148;
@@ -293,10 +304,19 @@ fdllm_status fdllm_decode_attention(const fdllm_decode* d, int32_t layer, const 
   a.k_stride = d->k_stride;
   a.v_stride = d->v_stride;
   a.unit_heads = group < kDecodeHeads ? group : kDecodeHeads;
+  bound_waits(a);
   cudaError_t e = launch_decode_attention(a, d->head_dim, d->dtype == FDLLM_F32, sms_here(),
                                           reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "decode_attention: launch");
   set_launch_count(2);
+  return FDLLM_OK;
+}
+
+fdllm_status fdllm_inject_tile_timeout(int64_t wait_ns) {
+  if (wait_ns < 0 || wait_ns > 1000000000)
+    return fail(FDLLM_ERR_INVALID_ARG, "inject_tile_timeout: wait of %lld ns outside [0, 10^9]",
+                (long long)wait_ns);
+  g_inject_wait_ns = wait_ns;
   return FDLLM_OK;
 }
 
@@ -358,6 +378,7 @@ fdllm_status fdllm_linear(const fdllm_linear_shape* s, const void* x, const void
   a.out_f32 = s->out_dtype == FDLLM_F32;
   a.ldr = s->ldr;
   a.ldy = s->ldy;
+  bound_waits(a);
   cudaError_t e = launch_linear(a, x, s->ldx, w, w_gate, sms_here(),
                                 reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "linear: launch");

@@ -56,6 +56,9 @@ struct FastDiv {
 #endif
 };
 
+// Bound of the kernels' waits, in cycles of the SM clock: about a second.
+constexpr long long kWaitCycles = 2000000000ll;
+
 // ---------------------------------------------------------------- block planning
 constexpr int kMaxPlanBatch = 16384;   // 12 bytes of shared memory per request
 
@@ -106,6 +109,8 @@ struct DecodeArgs {
   float* part;                // workspace
   unsigned long long* begun;  // behind the parts (see kBegun)
   int32_t* status;
+  long long wait_cycles;      // bound of a wait
+  int withhold;               // the first tile of every CTA is not said to be there (for tests)
   int batch, n_heads, n_kv_heads, group, head_chunks, units_per_seq;
   int max_blocks, num_pages, max_position, in_f32, out_bf16;
   FastDiv ps;
@@ -139,6 +144,8 @@ struct LinearArgs {
   int rows, n_in, n_out;
   int act, gated, bias_f32, out_f32;
   int64_t ldr, ldy;           // elements
+  int withhold;               // the first stage of every CTA is not said to be there (for tests)
+  long long wait_cycles;      // bound of a wait
 };
 
 cudaError_t launch_linear(const LinearArgs& a, const void* x, int64_t ldx, const void* w,
