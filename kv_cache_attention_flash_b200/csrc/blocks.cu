@@ -187,8 +187,9 @@ __global__ void __launch_bounds__(PT, 6) plan_kernel(const PlanArgs a) {
   // the rows to do
   const int step = gridDim.x * PT;
   const int n_pages = min(total_pages, n_free);
-  for (int p = step - 1 - (int)(blockIdx.x * PT + tid); p < n_pages; p += step) {
-    const int b = find(pages, B, p);
+  // (page counts reach 2^31 - 2, from where a step leaves int)
+  for (uint32_t at_page = step - 1 - (blockIdx.x * PT + tid); at_page < (uint32_t)n_pages; at_page += step) {
+    const int p = (int)at_page, b = find(pages, B, p);
     if (lens[b] < 0) continue;
     const int id = a.free_pages[n_free - 1 - p];
     const bool ok = id >= 0 && id < a.num_pages;
@@ -300,8 +301,8 @@ __global__ void __launch_bounds__(PT) release_kernel(const PlanArgs a) {
   }
   __syncthreads();
   const int n = min(total, room);
-  for (int p = blockIdx.x * PT + tid; p < n; p += gridDim.x * PT) {
-    const int b = find(pages, B, p);
+  for (uint32_t at_page = blockIdx.x * PT + tid; at_page < (uint32_t)n; at_page += gridDim.x * PT) {
+    const int p = (int)at_page, b = find(pages, B, p);
     const int id = a.table[(int64_t)b * a.max_blocks + kept[b] + p - pages[b]];
     const bool ok = id >= 0 && id < a.num_pages;
     if (!ok) report(a.status);
