@@ -131,7 +131,7 @@ __device__ __forceinline__ Seq seq_of(const DecodeArgs& a, int b) {
   }
   s.first = min(s.first, s.len);
   s.tile0 = s.first / TILE;
-  s.tiles = s.len > s.first ? (s.len + TILE - 1) / TILE - s.tile0 : 1;
+  s.tiles = tiles_of(s.first, s.len, TILE);
   return s;
 }
 
@@ -683,8 +683,10 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, const CUtensorMa
       for (int i = 0; i < seg; ++i) {
         const int key0 = (at.s.tile0 + at.t + i) * S::TILE;
         // runs: lane w < 4 looks up quarter w; by rows: lane r < KS row r of
-        // this warp's quarter
-        const int key = key0 + (kRows ? loader * S::KS + lane : lane * S::KS);
+        // this warp's quarter (the lanes beyond stay inside the tile: a slot
+        // behind the last tile may be past 2^31)
+        const int key = key0 + (kRows ? loader * S::KS + min(lane, S::KS - 1)
+                                      : min(lane, WARPS - 1) * S::KS);
         int row = -1;
         uint32_t seen = 0;              // runs: of quarter `lane`
         bool want = lane < S::KS && key < at.s.len && key >= at.s.first;

@@ -10,4 +10,10 @@ namespace fdllm {
 // returns at once while they are under way, and not at all once they are there.)
 constexpr int last_pass(int s, int next, int round) { return s < next ? round : round - 1; }
 
+// Tiles from that of slot `first` to that of slot len - 1, one where nothing is
+// visible (first == len). Lengths reach 2^31 - 2, so nothing is rounded up first.
+constexpr int tiles_of(int first, int len, int tile) {
+  return len > first ? (len - 1) / tile - first / tile + 1 : 1;
+}
+
 }  // namespace fdllm

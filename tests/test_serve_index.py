@@ -15,7 +15,7 @@ def host(tmp_path, body):
     if not shutil.which("g++"):
         pytest.skip("no g++")
     src, exe = tmp_path / "t.cpp", tmp_path / "t"
-    src.write_text('#include <cstdint>\n#include <cstdio>\n#include "serve_index.h"\nusing namespace fdllm;\n'
+    src.write_text('#include <cstdint>\n#include <cstdio>\n#include <initializer_list>\n#include "serve_index.h"\nusing namespace fdllm;\n'
                    '#define CHECK(x, ...) do { if (!(x)) { printf(__VA_ARGS__); return 1; } } while (0)\n'
                    "int main() {\n" + body + "\n  return 0;\n}\n")
     subprocess.run(["g++", "-std=c++17", "-O1", "-ftrapv", "-I", CSRC, str(src), "-o", str(exe)], check=True)
@@ -45,4 +45,26 @@ def test_the_last_pass_of_every_stage_of_a_ring(tmp_path):
         CHECK((under_way & 1) == parity, "the wait would return before the copies are there");
         CHECK((there & 1) != parity, "the wait would not return");
       }
+    }""")
+
+
+def test_the_tiles_of_a_range_of_slots(tmp_path):
+    """Against counting, and at lengths whose rounding up leaves 31 bits."""
+    host(tmp_path, """
+  for (int tile : {32, 64})
+    for (int first = 0; first <= 200; ++first)
+      for (int len = first; len <= 400; ++len) {
+        int seen = 0;
+        for (int t = 0; t * tile < 400; ++t) {
+          bool any = false;
+          for (int s = t * tile; s < (t + 1) * tile; ++s) any = any || (s >= first && s < len);
+          seen += any;
+        }
+        CHECK(tiles_of(first, len, tile) == (len > first ? seen : 1), "%d %d %d", first, len, tile);
+      }
+  const int most = 2147483646;
+  for (int tile : {32, 64})
+    for (int cut = 0; cut < 200; ++cut) {
+      const long long want = ((long long)most - cut + tile - 1) / tile;
+      CHECK(tiles_of(0, most - cut, tile) == want, "%d: %d", cut, tiles_of(0, most - cut, tile));
     }""")
