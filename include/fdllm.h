@@ -506,7 +506,8 @@ FDLLM_API fdllm_status fdllm_decode_attention(
 
 /* Activations: relu(a); silu(a) = a / (1 + e^-a); gelu(a) = a/2 (1 +
  * erf(a / sqrt 2)); gelu_tanh(a) = a/2 (1 + tanh(sqrt(2/pi) (a + 0.044715
- * a^3))). */
+ * a^3))). In fp32: silu to 2^-19 of its value; the gelus as written, to about
+ * 2^-22 of |a|, which for a below -3 or so is more than that of the value. */
 typedef enum {
   FDLLM_ACT_NONE = 0,
   FDLLM_ACT_RELU = 1,

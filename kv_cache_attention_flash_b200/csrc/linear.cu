@@ -55,7 +55,13 @@ constexpr int BOX = BK * 64 * 2;         // a box of W: 64 K rows x 64 columns, 
 __device__ __forceinline__ float activate(float x, int act) {
   switch (act) {
     case FDLLM_ACT_RELU: return x > 0.f ? x : (x == x ? 0.f : x);
-    case FDLLM_ACT_SILU: return __fdividef(x, 1.f + __expf(-x));
+    case FDLLM_ACT_SILU: {
+      // e = exp(-|x|) as a square: exp(x / 2) is a normal number down to x = -174,
+      // so x e keeps its bits where e itself would not. The divisor is in [1, 2],
+      // where the fast quotient is good to two steps.
+      const float t = expf(-0.5f * fabsf(x)), e = t * t;
+      return __fdividef(x < 0.f ? x * t * t : x, 1.f + e);
+    }
     case FDLLM_ACT_GELU: return 0.5f * x * (1.f + erff(x * 0.7071067811865476f));
     case FDLLM_ACT_GELU_TANH:
       return 0.5f * x * (1.f + tanhf(0.7978845608028654f * fmaf(0.044715f * x * x, x, x)));
