@@ -284,8 +284,9 @@ def _is_f32(dtype) -> bool:
 
 
 def fdllm_plan_buffers(batch: int, capacity: int, device="cuda") -> dict:
-    """The outputs of fdllm_plan_blocks for up to `batch` requests' worth of
-    lengths and `capacity` rows, to be kept and passed as `out`."""
+    """The outputs of fdllm_plan_blocks for `batch` requests (no more and no
+    fewer: slices of larger ones will do) and up to `capacity` rows, to be kept
+    and passed as `out`."""
     i32 = dict(dtype=torch.int32, device=device)
     return {"cu_rows": torch.empty(batch + 1, **i32), "positions": torch.empty(capacity, **i32),
             "slots": torch.empty(capacity, **i32), "row_seq": torch.empty(capacity, **i32),

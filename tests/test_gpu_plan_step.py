@@ -115,3 +115,21 @@ def test_refusals_of_the_two_outputs():
         assert plan(**{n: 8 * MB}) == BAD and b"overlaps" in lib.fdllm_last_error()
     assert plan(seq_slots=15 * MB) == BAD and b"overlaps" in lib.fdllm_last_error()
     assert lib.fdllm_plan_step(0, 4, 16, 8, 10, *[ctypes.c_void_p(MB)] * 17, None) == BAD
+
+
+@pytest.mark.gpu
+def test_buffers_are_for_exactly_their_batch():
+    """Buffers of four requests are refused for three; slices of them serve."""
+    lens, new, table, free = dev([3, 0, 8]), dev([1, 2, 0]), dev([[0, 9], [9, 9], [1, 2]]), dev([5, 4, 3])
+    out = fd.fdllm_plan_buffers(4, 10)
+    with pytest.raises(ValueError, match="shape"):
+        fd.fdllm_plan_blocks(lens, new, table, 4, free, dev([2]), out=out)
+    part = {k: v[:{"cu_rows": 4, "seq_lens": 3, "granted": 3, "seq_positions": 3, "seq_slots": 3}.get(k, len(v))]
+            for k, v in out.items()}
+    fd.fdllm_plan_blocks(lens, new, table, 4, free, dev([2]), out=part)
+    assert out["cu_rows"][:4].tolist() == [0, 1, 3, 3] and out["seq_lens"][:3].tolist() == [4, 2, 8]
+    assert out["seq_slots"][:3].tolist() == [3, 1, -1] and out["slots"][:3].tolist() == [3, 0, 1]
+    # without the entries that may be left out
+    few = {k: v for k, v in part.items() if k not in ("headroom", "seq_positions", "seq_slots")}
+    table = dev([[0, 9], [9, 9], [1, 2]])
+    assert fd.fdllm_plan_blocks(lens, new, table, 4, free, dev([2]), out=few)["seq_lens"].tolist() == [4, 2, 8]
