@@ -3,6 +3,7 @@
 // synchronises or throws.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -265,7 +266,9 @@ fdllm_status fdllm_decode_attention(const fdllm_decode* d, int32_t layer, const 
                         {k, ((rows - 1) * d->k_stride + hk) * in},
                         {v, ((rows - 1) * d->v_stride + hk) * in},
                         {positions, rows * 4}, {slots, rows * 4}, {seq_lens, rows * 4},
-                        {starts, rows * 4}, {block_table, rows * d->max_blocks_per_seq * 4}};
+                        {starts, rows * 4}, {block_table, rows * d->max_blocks_per_seq * 4},
+                        {rope_cos, (uint64_t)std::max(d->max_position, 0) * d->head_dim * 4},
+                        {rope_sin, (uint64_t)std::max(d->max_position, 0) * d->head_dim * 4}};
     if (any_meet(outs, ins))
       return fail(FDLLM_ERR_INVALID_ARG, "decode_attention: an output overlaps another argument");
   }
