@@ -537,7 +537,10 @@ typedef struct {
 /* y = residual + act(x w + bias), or with w_gate
  * y = residual + act(x w_gate + bias_gate) * (x w + bias): a layer's
  * projections and the first half of its (gated) feed-forward block, in one
- * launch. fdllm_oproj is its special case of a square w.
+ * launch. fdllm_oproj is its special case of a square w. This call is the
+ * faster one but for 1000 to 1500 rows of small squares (4096 x 4096: 9.7 us
+ * against 24 for one row, 18 against 26 for 256, 99 against 127 for 4096;
+ * 1024 x 1024: 4.4 against 8.4 for one row, 11.5 against 10.4 for 1536).
  *   x: DEVICE bf16 [rows][n_in]. w, w_gate: DEVICE bf16 [n_in][n_out],
  *     row-major and contiguous (y = x W, as wqkv); w_gate may be NULL.
  *   bias, bias_gate: DEVICE [n_out] of bias_dtype, or NULL; bias_gate needs

@@ -36,8 +36,8 @@
 //     of eight tiles at least, taken over from the grid as CTAs get on: SMs do
 //     not stream at one speed.
 //   - bf16 products by m16n8k16 warp MMAs: eight heads are far too few rows
-//     for tcgen05's 128, and the products are a tenth of the issue slots that
-//     the loads leave free. The cache's rows are the A operand (16 slots, then
+//     for tcgen05's 128, and the bytes bound them (the tensor pipe is active in
+//     a fifth of the cycles, ncu). The cache's rows are the A operand (16 slots, then
 //     16 dimensions), the heads B's eight columns; each fp32 value of q and
 //     then of P enters as a bf16 pair hi + lo, a product each, which keeps 16
 //     bits of it. Every thread holds two heads, whose statistics, scores and O
@@ -48,10 +48,14 @@
 //     memory for the tile that it belongs to.
 //
 // Measured on one B200, both launches, back to back, head_dim 128: two sequences
-// of 120 to 131 thousand slots, 8 key heads: 158 us (6.5 TB/s, the rate of a copy);
-// 32 of 256 to 1024 slots, 32 key heads: 61.6 us (5.5 TB/s; an end of a unit costs
-// a CTA's computing warps 1.5 us); one of 768: 8.6 us (latency); fp32, 61 sequences,
-// pages of 6, head_dim 96: 48 us (4.4 TB/s; row copies and fp32 FMAs).
+// of 120 to 131 thousand slots, 8 key heads: 157 to 159 us (6.5 TB/s, the rate of a
+// copy); 32 of 256 to 1024 slots, 32 key heads: 60.7 us (5.5 TB/s; an end of a unit
+// costs a CTA's computing warps 1.5 us); one of 768: 8.5 to 8.8 us (latency); fp32, 61
+// sequences, pages of 6, head_dim 96: 48.6 us (4.4 TB/s; row copies and fp32 FMAs);
+// fp32, 16 of 1024 to 4096, 8 key heads, pages of 64: 56 us with one head each and 59
+// with four (6.0 and 5.7 TB/s), 91 with eight (3.7 TB/s: one CTA an SM, and FMAs).
+// K and V are read once for every eight heads of a key head: four sequences of 60 to
+// 66 thousand slots, one key head: 31 us with 8 heads, 37 with 16, 69 with 32.
 #include <cuda_bf16.h>
 
 #include <cstdint>
@@ -205,7 +209,10 @@ struct Ctrl {
 };
 
 // 32 sequences of the line, one a lane, kept by a warp: what a batch of up to
-// 32 needs is read once.
+// 32 needs is read once. A larger one is walked through, 32 at a time, by every
+// loading warp (for the line's length, then for its share's place) and every
+// joining one, which short sequences do not cover: 1000 of up to 1024 slots, 8 key
+// heads, 510 us (6.2 TB/s), of up to 128 slots 136 us, of up to 16 slots 110 us.
 template <int TILE>
 struct Window {
   Seq own;
@@ -1144,6 +1151,10 @@ cudaError_t launch(const DecodeArgs& a, int sms, cudaStream_t stream) {
     b.slot_bytes = b.rope_at + (a.rope_cos ? D * 8 : 0);
     return 2 * (fixed + S::STAGES * b.slot_bytes + rotated + own + 1024) <= 228 * 1024;
   };
+  // (One CTA an SM remains for fp32 q of 8 heads a key head at head_dim 128: over a
+  // bf16 cache of 8 key heads, 32 sequences of 512 to 2048 slots, 53.0 us instead of
+  // the 44.6 of bf16 q, 2 of 60 to 66 thousand 88.3 instead of 84.0; and for fp32
+  // caches of 5 to 8 heads.)
   const bool two = lay_out(a.k != nullptr) || lay_out(false);
   b.resident = two ? 2 * sms : sms;
   const int bytes = fixed + S::STAGES * b.slot_bytes + rotated;

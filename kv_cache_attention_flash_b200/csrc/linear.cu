@@ -29,11 +29,12 @@
 // Both start under the tail of the launch before them (dependent launch): the
 // barriers, the TMEM and the tensor maps are ready when its results are.
 //
-// Measured on one B200, launches back to back: wide, 8192 rows, 4096 -> 12288 with
-// gelu: 577 to 610 us (1430 to 1350 TFLOP/s, power); gated, 1536 rows: 191 us
-// (1620 TFLOP/s, tensor pipe 95 % active); 1001 rows, 1304 -> 2696: 16 us, of which 7
-// are fill and epilogue. Narrow, one row, 4096 -> 4096: 9.9 us (3.4 TB/s); to 12288:
-// 20.1 us (5.0 TB/s); gated, 32 rows: 36.5 us (5.5 TB/s).
+// Measured on one B200, device time of launches back to back: wide, 8192 rows, 4096 ->
+// 12288 with gelu: 579 to 640 us (1420 to 1290 TFLOP/s, as the power limit leaves);
+// gated, 1536 rows: 189 to 199 us (1640 to 1560 TFLOP/s, tensor pipe 95 % active), 224
+// to 232 in minutes of such calls; 1001 rows, 1304 -> 2696: 16.0 us, of which 7 are fill
+// and epilogue. Narrow, one row, 4096 -> 4096: 9.8 us (3.4 TB/s); to 12288: 20.1 us
+// (5.0 TB/s); gated, 32 rows: 36.9 us (5.5 TB/s).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
