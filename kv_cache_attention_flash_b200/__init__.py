@@ -28,7 +28,8 @@ __all__ = [
     "fdllm_select_tracked", "fdllm_verify_accept", "fdllm_plan_tile_schedule", "fdllm_oproj",
     "fdllm_plan_blocks", "fdllm_release_blocks", "fdllm_plan_buffers", "fdllm_decode_attention",
     "fdllm_rope_tables", "fdllm_linear",
-    "fdllm_check", "fdllm_inject_fault", "fdllm_inject_tile_timeout", "fdllm_last_launch_count", "FlashCache", "FdllmError",
+    "fdllm_check", "fdllm_inject_fault", "fdllm_inject_tile_timeout", "fdllm_last_launch_count",
+    "FlashCache", "FdllmError",
     "load",
 ]
 
